@@ -319,8 +319,9 @@ __device__ __forceinline__ void mod_rows_cap(uint32_t ts, uint32_t to, bool firs
   const float far = fmaxf(mx, -lo) * a.c;
   const int form =
       __all_sync(0xffffffffu, far <= TANH_NEAR) ? CAP_NEAR : (__all_sync(0xffffffffu, far <= 1.0f) ? CAP_POLY : CAP_EXP);
-  // (the cap is monotonic: the maximum is taken before it)
-  mx = mx == neg_inf() ? mx : a.cap2 * tanh_score(mx * a.c);
+  // (the cap is monotonic: the maximum is taken before it.  A visible product of -inf is a score of -cap: a row is
+  // without a maximum only where it sees no key of the block)
+  mx = seen == 0 ? neg_inf() : a.cap2 * tanh_score(mx * a.c);
   float alpha = 1.0f;
   if (mx > m_ref + 8.0f) {
     alpha = m_ref == neg_inf() ? 0.0f : ex2_full(m_ref - mx);
