@@ -88,11 +88,13 @@ struct MbwCols {
 };
 
 // P of the thread's 32 columns from the raw products y: p, and packed in the input type pk2. With a cap
-// MODE_DKV needs P (1 - t^2) alone further on (p holds that), MODE_DQ both: t2 keeps t^2 as fp16 pairs
-// (off by 2^-12 t^2, small beside dS's own rounding).
+// MODE_DKV needs P (1 - t^2) alone further on (p holds that), MODE_DQ both: w2 keeps 1 - t^2 as fp16 pairs.
+// (The factor itself, not t^2: it is off by 2^-11 of its value at most, what dS's own rounding costs in fp16 and
+// an eighth of that in bf16, and by 2^-25 where it is subnormal, less than t's own last bit leaves of it.  t^2 in fp16
+// would be off by 2^-12 beside a factor that vanishes at the cap: dq was up to 149 times its bound.)
 template <typename T, int MODE, bool CAP, bool BIAS, int FORM, bool BORDER, int LINE>
 __device__ __forceinline__ void mbw_probs(float (&p)[32], const ModArgs& a, const MbwCols& q,
-                                          uint32_t (&t2)[CAP && MODE == MODE_DQ ? 16 : 1], uint32_t (&pk2)[16]) {
+                                          uint32_t (&w2)[CAP && MODE == MODE_DQ ? 16 : 1], uint32_t (&pk2)[16]) {
   // LINE: 1 the distance falls (MODE_DQ) or rises along the columns, 0 it turns within them
   const float step = MODE == MODE_DQ ? -1.0f : 1.0f;
   const float st = -q.slope2 * step, base = -q.slope2 * q.d0;
@@ -140,7 +142,8 @@ __device__ __forceinline__ void mbw_probs(float (&p)[32], const ModArgs& a, cons
     if constexpr (!CAP) {
       pk2[x / 2] = pack2<T>(p0, p1);
     } else {
-      const unsigned long long pd = mul2(pk(p0, p1), fma2(tt, pk(-1.0f, -1.0f), pk(1.0f, 1.0f)));
+      const unsigned long long w = fma2(tt, pk(-1.0f, -1.0f), pk(1.0f, 1.0f));
+      const unsigned long long pd = mul2(pk(p0, p1), w);
       if constexpr (MODE == MODE_DKV) {
         pk2[x / 2] = pack2<T>(p0, p1);
         p[x] = pk_lo(pd);
@@ -148,7 +151,7 @@ __device__ __forceinline__ void mbw_probs(float (&p)[32], const ModArgs& a, cons
       } else {
         // X1 takes P (1 - t^2): the correction it serves is one of dS
         pk2[x / 2] = pack2<T>(pk_lo(pd), pk_hi(pd));
-        t2[x / 2] = pack2<__half>(pk_lo(tt), pk_hi(tt));
+        w2[x / 2] = pack2<__half>(pk_lo(w), pk_hi(w));
       }
     }
   }
@@ -156,22 +159,22 @@ __device__ __forceinline__ void mbw_probs(float (&p)[32], const ModArgs& a, cons
 
 template <typename T, int MODE, bool CAP, bool BIAS, int FORM, bool BORDER>
 __device__ __forceinline__ void mbw_probs_line(float (&p)[32], const ModArgs& a, const MbwCols& q, int line,
-                                               uint32_t (&t2)[CAP && MODE == MODE_DQ ? 16 : 1], uint32_t (&pk2)[16]) {
+                                               uint32_t (&w2)[CAP && MODE == MODE_DQ ? 16 : 1], uint32_t (&pk2)[16]) {
   if constexpr (!BIAS) {
-    mbw_probs<T, MODE, CAP, BIAS, FORM, BORDER, 0>(p, a, q, t2, pk2);
+    mbw_probs<T, MODE, CAP, BIAS, FORM, BORDER, 0>(p, a, q, w2, pk2);
   } else {
     // (a line that rises against the usual direction takes the general form)
     if (__builtin_expect(line > 0, 1))
-      mbw_probs<T, MODE, CAP, BIAS, FORM, BORDER, 1>(p, a, q, t2, pk2);
+      mbw_probs<T, MODE, CAP, BIAS, FORM, BORDER, 1>(p, a, q, w2, pk2);
     else
-      mbw_probs<T, MODE, CAP, BIAS, FORM, BORDER, 0>(p, a, q, t2, pk2);
+      mbw_probs<T, MODE, CAP, BIAS, FORM, BORDER, 0>(p, a, q, w2, pk2);
   }
 }
 
 // Scores to P, over the first 16 of the score columns they came from
 template <typename T, int MODE, bool CAP, bool BIAS>
 __device__ __forceinline__ void mbw_phase1(uint32_t ts, const ModArgs& a, const MbwCols& q, bool border, int line,
-                                           float (&p)[32], uint32_t (&t2)[CAP && MODE == MODE_DQ ? 16 : 1]) {
+                                           float (&p)[32], uint32_t (&w2)[CAP && MODE == MODE_DQ ? 16 : 1]) {
   tc_ld32(ts, p);
   int form = CAP_EXP;
   if constexpr (CAP) {
@@ -184,16 +187,16 @@ __device__ __forceinline__ void mbw_phase1(uint32_t ts, const ModArgs& a, const 
   }
   uint32_t pk2[16];
   if (__builtin_expect(!border && (!CAP || form == CAP_NEAR), 1)) {
-    mbw_probs_line<T, MODE, CAP, BIAS, CAP_NEAR, false>(p, a, q, line, t2, pk2);
+    mbw_probs_line<T, MODE, CAP, BIAS, CAP_NEAR, false>(p, a, q, line, w2, pk2);
   } else if (border) {
     if (CAP && form != CAP_EXP)
-      mbw_probs_line<T, MODE, CAP, BIAS, CAP_POLY, true>(p, a, q, line, t2, pk2);
+      mbw_probs_line<T, MODE, CAP, BIAS, CAP_POLY, true>(p, a, q, line, w2, pk2);
     else
-      mbw_probs_line<T, MODE, CAP, BIAS, CAP_EXP, true>(p, a, q, line, t2, pk2);
+      mbw_probs_line<T, MODE, CAP, BIAS, CAP_EXP, true>(p, a, q, line, w2, pk2);
   } else if (CAP && form == CAP_POLY) {
-    mbw_probs_line<T, MODE, CAP, BIAS, CAP_POLY, false>(p, a, q, line, t2, pk2);
+    mbw_probs_line<T, MODE, CAP, BIAS, CAP_POLY, false>(p, a, q, line, w2, pk2);
   } else if (CAP) {
-    mbw_probs_line<T, MODE, CAP, BIAS, CAP_EXP, false>(p, a, q, line, t2, pk2);
+    mbw_probs_line<T, MODE, CAP, BIAS, CAP_EXP, false>(p, a, q, line, w2, pk2);
   }
   tc_st16u(ts, pk2);
 }
@@ -201,7 +204,7 @@ __device__ __forceinline__ void mbw_phase1(uint32_t ts, const ModArgs& a, const 
 // dS = P (1 - t^2) (dP - D) over the first 16 columns of the dP it came from; MODE_DQ: r += P (dP - D)
 template <typename T, int MODE, bool CAP>
 __device__ __forceinline__ void mbw_phase2(uint32_t tdp, float delta, uint32_t stats, const float (&p)[32],
-                                           const uint32_t (&t2)[CAP && MODE == MODE_DQ ? 16 : 1], float& r) {
+                                           const uint32_t (&w2)[CAP && MODE == MODE_DQ ? 16 : 1], float& r) {
   const unsigned long long nd = pk(-delta, -delta);
   unsigned long long acc[2] = {0ull, 0ull};
   float dp[32];
@@ -219,8 +222,8 @@ __device__ __forceinline__ void mbw_phase2(uint32_t tdp, float delta, uint32_t s
     if constexpr (MODE == MODE_DQ) acc[(x >> 1) & 1] = fma2(pp, v, acc[(x >> 1) & 1]);
     unsigned long long d = mul2(pp, v);
     if constexpr (CAP && MODE == MODE_DQ) {
-      const float2 tt = __half22float2(*reinterpret_cast<const __half2*>(&t2[x / 2]));
-      d = mul2(d, fma2(pk(tt.x, tt.y), pk(-1.0f, -1.0f), pk(1.0f, 1.0f)));
+      const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&w2[x / 2]));
+      d = mul2(d, pk(w.x, w.y));
     }
     ds[x / 2] = pack2<T>(pk_lo(d), pk_hi(d));
   }
@@ -593,17 +596,17 @@ __global__ void __launch_bounds__(MBW_THREADS, 1)
         line = __all_sync(0xffffffffu, ahead) ? 1 : 0;
       }
       float p[32];
-      uint32_t t2[CAP && MODE == MODE_DQ ? 16 : 1];
+      uint32_t w2[CAP && MODE == MODE_DQ ? 16 : 1];
       wait_or_flag(B_S + grp, (uint32_t)((i >> 1) & 1));
       if constexpr (MODE == MODE_DKV) wait_or_flag(B_C1 + i % NST, (uint32_t)((i / NST) & 1));  // the statistics
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      mbw_phase1<T, MODE, CAP, BIAS>(ts, a, cq, border, line, p, t2);
+      mbw_phase1<T, MODE, CAP, BIAS>(ts, a, cq, border, line, p, w2);
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_P + grp));
       wait_or_flag(B_DP + grp, (uint32_t)((i >> 1) & 1));
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      mbw_phase2<T, MODE, CAP>(tdp, delta, stats + 256, p, t2, r);
+      mbw_phase2<T, MODE, CAP>(tdp, delta, stats + 256, p, w2, r);
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_DS + grp));

@@ -21,8 +21,8 @@ w = 1 - t^2; 1 and 0 in their place without a cap):
   dS         (h + p_i) |dS| + z + 2^-126 w (|dP| + |D|) + P w (u (D + 2) |do|.|v| + e_d + 2 h e_o + 16 u (|dP| + |D|))
              + P e_w (|dP| + |D|)
              (2 h e_o: dS is rounded to the type before the correction, and so is the P w that carries it)
-  dS for dq  the factor w is kept as fp16 between two steps: 2^-12 |dS| more, and 2^-25 P (|dP| + |D|) where it is
-             subnormal
+  dS for dq  the factor w is kept as fp16 between two steps: 2^-11 |dS| more (fp16 steps by 2^-10, half of it is the
+             rounding), and 2^-25 P (|dP| + |D|) where it is subnormal (steps of 2^-24)
   dq         scale (sum_j e_dS |k| + u n sum_j |dS| |k|) + h |dq| + z;  dk likewise over i
 """
 import math
@@ -91,7 +91,7 @@ def reference(q, k, v, scale, seen, pos, softcap=0.0, slopes=None, d_o=None):
     ed = pi * (p * (dP - delta).abs()).sum(-1, keepdim=True) + (p * (prod + U * (m + 16) * size)).sum(-1, keepdim=True)
     dsb = (h + pi) * dS.abs() + torch.where(sn, z, 0.0) + 2.0 ** -126 * w * size \
         + p * w * (prod + ed + 2 * h * eo + 16 * U * size) + p * ew * size
-    dqs = dsb + (2.0 ** -12 * dS.abs() + 2.0 ** -25 * p * size if softcap > 0 else 0.0)
+    dqs = dsb + (2.0 ** -11 * dS.abs() + 2.0 ** -25 * p * size if softcap > 0 else 0.0)
     dq = scale * (dS @ kd)
     dqb = scale * ((dqs + U * m * dS.abs()) @ kd.abs()) + h * dq.abs() + z
     dk = scale * group(dS.transpose(-1, -2) @ qd)

@@ -72,3 +72,13 @@ def test_an_infinite_key_under_a_cap(dt, n, D):
     k[0, :, :130, 0] = float("inf")
     k[1, :, 100:, 0] = float("inf")
     compare(q, k, v, softcap=7.0)
+
+
+@pytest.mark.parametrize("std,cap", [(20.0, 20.0), (60.0, 20.0), (150.0, 50.0), (30.0, 5.0), (3.0, 50.0)])
+@pytest.mark.parametrize("n,m,D", [(150, 210, 64), (16, 16, 128), (300, 300, 128), (4, 3, 64)])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_gradients_where_a_cap_saturates(std, cap, n, m, D, dt):
+    """Raw scores up to several times the cap, rows of few keys and of many."""
+    q, k, v, d_o, _ = make(int(std) + n, 2, 4, 2, n, m, D, dt, std=std)
+    compare(q, k, v, d_o, causal=m >= n, softcap=cap)
+    compare(q, k, v, d_o, causal=m >= n, softcap=cap, slopes=slopes_of(4))
