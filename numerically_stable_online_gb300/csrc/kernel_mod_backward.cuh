@@ -24,7 +24,8 @@
 // D: do . o uses o as it was rounded, which is what is left of the error of rows
 // that attend to few keys (measured on such rows: 1.5 times the error of the result's own
 // rounding).  MODE_DQ therefore sums r = sum_j P (dP - D~) = D - D~ in fp32, corrects its
-// result by -r sum_j P k_j (X1, one product more) and leaves D~ + r for MODE_DKV, which runs after it.
+// result by -r sum_j P k_j (X1, one product more) and leaves D~ + r for MODE_DKV, which runs after it.  (Hence o
+// and the LSE have to be the forward's over these very keys: sum_j P = 1.)
 //
 // A lane whose result is not finite is computed again from the pairs that are visible
 // (kernel_mod_exact.cuh).  Bound: at D = 128 the products, four a block (1280 tensor cycles, the 64-column ones at two
@@ -285,13 +286,15 @@ __device__ __noinline__ void mbw_exact(const ModBwdKernelArgs& f, int b, int h, 
   constexpr int N = D / 32;
   if constexpr (MODE == MODE_DQ) {
     const int u = h / a.group;
-    float acc[N];
+    float acc[N], delta;
     mod_exact_dq_row<T, D>(a, q + b * a.qs[0] + h * a.qs[1] + at * a.qs[2],
                            d_o + b * f.m.dos[0] + h * f.m.dos[1] + at * f.m.dos[2],
                            o + b * a.os[0] + h * a.os[1] + at * a.os[2], k + b * a.ks[0] + u * a.ks[1],
                            v + b * a.vs[0] + u * a.vs[1], a.k_doc != nullptr ? a.k_doc + (int64_t)b * a.sk : nullptr,
                            mod_view(a, b, at), a.slopes != nullptr ? a.slopes[h] * L2E_HI : 0.0f,
-                           lse[((int64_t)b * a.hq + h) * a.sq + at] * L2E_HI, acc);
+                           lse[((int64_t)b * a.hq + h) * a.sq + at] * L2E_HI, acc, delta);
+    // (the D that MODE_DKV reads: one NaN there would send all keys of its block here too)
+    if ((threadIdx.x & 31) == 0) f.delta[((int64_t)b * a.hq + h) * f.sq_pad + at] = delta;
 #pragma unroll
     for (int x = 0; x < N; ++x) acc[x] *= f.m.scale;
     mod_row_store<T, D>(out1 + b * f.m.dqs[0] + h * f.m.dqs[1] + at * f.m.dqs[2], acc);
@@ -306,7 +309,8 @@ __device__ __noinline__ void mbw_exact(const ModBwdKernelArgs& f, int b, int h, 
     if (kdoc >= 0 && at < mod_klen(a, b))
       for (int hh = u * a.group; hh < (u + 1) * a.group; ++hh)
         mod_exact_dkv_head<T, D>(a, q + b * a.qs[0] + hh * a.qs[1], d_o + b * f.m.dos[0] + hh * f.m.dos[1],
-                                 o + b * a.os[0] + hh * a.os[1], lse + ((int64_t)b * a.hq + hh) * a.sq, f.m.dos, b, at,
+                                 f.delta + ((int64_t)b * a.hq + hh) * f.sq_pad, lse + ((int64_t)b * a.hq + hh) * a.sq,
+                                 f.m.dos, b, at,
                                  kdoc, a.slopes != nullptr ? a.slopes[hh] * L2E_HI : 0.0f, kr, vr, gk, gv);
 #pragma unroll
     for (int x = 0; x < N; ++x) gk[x] *= f.m.scale;

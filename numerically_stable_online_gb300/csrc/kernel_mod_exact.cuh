@@ -90,20 +90,22 @@ __device__ __forceinline__ float mod_prob(float y, float lse2) {
   return lse2 == neg_inf() || y == neg_inf() ? 0.0f : ex2_full(y - lse2);
 }
 
-// dq of one row over its visible keys
+// dq of one row over its visible keys, and its D: do . o with o as it was rounded, corrected by r = sum P (dP - D) as
+// the tensor-core kernel does (dq by -r sum P (1 - t^2) k).  A row without visible keys has D = 0, whatever do holds.
 template <typename T, int D>
 __device__ void mod_exact_dq_row(const ModArgs& a, const T* qrow, const T* dorow, const T* orow, const T* kh,
                                  const T* vh, const int32_t* kdoc, const ModView& v, float slope2, float lse2,
-                                 float (&dq)[D / 32]) {
+                                 float (&dq)[D / 32], float& delta) {
   constexpr int N = D / 32;
-  float q[N], g[N], o[N];
+  float q[N], g[N], o[N], w[N], r = 0.0f;
   mod_row_load<T, D>(qrow, q);
   mod_row_load<T, D>(dorow, g);
   mod_row_load<T, D>(orow, o);
 #pragma unroll
-  for (int i = 0; i < N; ++i) dq[i] = 0.0f;
-  if (v.lim <= 0) return;
-  const float delta = mod_dot(g, o);
+  for (int i = 0; i < N; ++i) dq[i] = w[i] = 0.0f;
+  delta = 0.0f;
+  if (v.lim <= 0 || lse2 == neg_inf()) return;
+  delta = mod_dot(g, o);
   for (int64_t j = 0; j < v.lim; ++j) {
     if (kdoc != nullptr && kdoc[j] != v.doc) continue;
     float k[N], vr[N];
@@ -115,17 +117,24 @@ __device__ void mod_exact_dq_row(const ModArgs& a, const T* qrow, const T* dorow
     const float p = mod_prob(y, lse2);
     const float dp = mod_dot(g, vr);
     if (p == 0.0f) continue;
-    const float ds = p * (dp - delta) * deriv;
+    const float pv = p * (dp - delta), ds = pv * deriv, pw = p * deriv;
+    r += pv;
 #pragma unroll
-    for (int i = 0; i < N; ++i) dq[i] = __fmaf_rn(ds, k[i], dq[i]);
-    if (ds != ds) return;
+    for (int i = 0; i < N; ++i) {
+      dq[i] = __fmaf_rn(ds, k[i], dq[i]);
+      w[i] = __fmaf_rn(pw, k[i], w[i]);
+    }
+    if (ds != ds) break;  // NaN in all of dq, and in r
   }
+#pragma unroll
+  for (int i = 0; i < N; ++i) dq[i] = __fmaf_rn(-r, w[i], dq[i]);
+  delta += r;
 }
 
-// dk and dv of key j of one query head, added to what the arrays hold; ends where all of them are NaN (as they
+// dk and dv of key j of one query head, added to what the arrays hold, with the rows' D (delta); ends where all of them are NaN (as they
 // are once a NaN row sees the key: nothing after it changes them)
 template <typename T, int D>
-__device__ void mod_exact_dkv_head(const ModArgs& a, const T* qh, const T* doh, const T* oh, const float* lse,
+__device__ void mod_exact_dkv_head(const ModArgs& a, const T* qh, const T* doh, const float* delta, const float* lse,
                                    const int64_t (&dos)[3], int b, int64_t j, int kdoc, float slope2,
                                    const float (&k)[D / 32], const float (&vr)[D / 32], float (&dk)[D / 32],
                                    float (&dv)[D / 32]) {
@@ -133,15 +142,14 @@ __device__ void mod_exact_dkv_head(const ModArgs& a, const T* qh, const T* doh, 
   for (int64_t i = 0; i < a.sq; ++i) {
     const ModView v = mod_view(a, b, i);
     if (j >= v.lim || v.doc != kdoc) continue;
-    float q[N], g[N], o[N];
+    float q[N], g[N];
     mod_row_load<T, D>(qh + i * a.qs[2], q);
     mod_row_load<T, D>(doh + i * dos[2], g);
-    mod_row_load<T, D>(oh + i * a.os[2], o);
     float deriv;
     float y = mod_score(a, mod_dot(q, k), deriv);
     if (slope2 != 0.0f) y += mod_bias(slope2, v.pos, j);
     const float p = mod_prob(y, lse[i] * L2E_HI);
-    const float ds = p == 0.0f ? 0.0f : p * (mod_dot(g, vr) - mod_dot(g, o)) * deriv;
+    const float ds = p == 0.0f ? 0.0f : p * (mod_dot(g, vr) - delta[i]) * deriv;
 #pragma unroll
     for (int x = 0; x < N; ++x) {
       if (p != 0.0f) {
