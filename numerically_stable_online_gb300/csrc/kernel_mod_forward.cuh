@@ -16,8 +16,8 @@
 //     the maximum; only blocks at a mask's border test keys one by one;
 //   - a row's keys may be split over items (few rows, many keys): each part leaves its
 //     unnormalised (m, l, o) in fp32 and k_mod_merge joins them in order;
-//   - a row whose result is not finite is computed again from the keys it sees
-//     (kernel_mod_exact.cuh): a product's 0 x NaN from a key that the row does not see leaves no trace.
+//   - a row whose result is not finite is computed again from the keys it sees, behind the CTA's items
+//     (mod_fix_items, kernel_mod_exact.cuh): a product's 0 x NaN from a key that the row does not see leaves no trace.
 //
 // Bound: at D = 128 the tensor cores (2 x 32 heads x 4096 rows: 369 us, 1490 TFLOP/s; causal 211 us); a cap, a bias or
 // D = 64 makes it the row warps' arithmetic (the exp2 unit and issue slots; capped 629 us, causal 357; slopes 524,
@@ -177,6 +177,50 @@ struct ModRowState {
   float slope2;   // base-2 slope
   int64_t pos;
 };
+
+// Row rt of an item's tile t: query i of head h, its place among all rows of the result, its query's offset.
+// Rows past the end stand for the last row (in false: nothing of theirs is stored).
+struct ModRowAt {
+  bool in;
+  int h;
+  int64_t i, lse_at, qoff;
+  ModRowState rs;
+};
+template <bool BIAS>
+__device__ __forceinline__ ModRowAt mod_row_at(const ModFwdArgs& f, const ModItem& it, int t, int rt) {
+  const ModArgs& a = f.a;
+  ModRowAt x;
+  const int64_t r = it.r0 + t * ATM_BM + rt;
+  x.in = r < f.rows;
+  const int64_t rc = x.in ? r : f.rows - 1;
+  const int g = f.pf > 1 ? (int)((uint32_t)rc / (uint32_t)a.sq) : 0;
+  x.i = rc - (int64_t)g * a.sq;
+  x.h = it.hp * f.pf + g;
+  x.lse_at = ((int64_t)it.b * a.hq + x.h) * a.sq + x.i;
+  x.qoff = it.b * a.qs[0] + (int64_t)x.h * a.qs[1] + x.i * a.qs[2];
+  if (f.req > 0) {
+    const int per = f.map_group * f.map_sq, rq = (int)rc / per, rest = (int)rc - rq * per;
+    const int hg = rest / f.map_sq, tok = rest - hg * f.map_sq, hh = it.u * f.map_group + hg;
+    x.lse_at = ((int64_t)rq * f.map_hq + hh) * f.map_sq + tok;
+    if (f.q_req) x.qoff = (int64_t)rq * a.qs[0] + (int64_t)hh * a.qs[1] + tok * a.qs[2];
+    int64_t own = f.own_sk;
+    if (f.own_len != nullptr) {
+      const int64_t y = f.own_len[rq];
+      own = y < 0 ? 0 : (y < own ? y : own);
+    }
+    x.rs.pos = a.sk + own - f.map_sq + tok;
+    x.rs.lim = (int)a.sk;
+    x.rs.doc = 0;
+    x.rs.slope2 = BIAS ? a.slopes[hh] * L2E_HI : 0.0f;
+  } else {
+    const ModView view = mod_view(a, it.b, x.i);
+    x.rs.pos = view.pos;
+    x.rs.lim = (int)view.lim;
+    x.rs.doc = view.doc;
+    x.rs.slope2 = BIAS ? a.slopes[x.h] * L2E_HI : 0.0f;
+  }
+  return x;
+}
 
 // Keys of a block of 64 below the row's limit, as a bit mask.
 __device__ __forceinline__ uint64_t mod_block_seen(const ModRowState& rs, int key0) {
@@ -467,44 +511,64 @@ __device__ __forceinline__ void mod_rows_block(uint32_t ts, uint32_t to, bool fi
   tc_st32(ts, pk2);
 }
 
-// The rows of a warp whose results are not finite, again from the keys they
-// see (rare: a NaN or an infinity among the inputs).  bad: the lanes; each
-// lane's row: its position, limit, document and slope, its query's and its output's offset, its index among all rows.
-template <typename T, int D>
-__device__ __noinline__ void mod_fix_rows(uint32_t bad, const ModFwdArgs& f, int batch, int u, int first, int nmax,
-                                          int split, int64_t pos, int lim, int doc, float slope, int64_t qoff,
-                                          int64_t ooff, const T* q, const T* k, const T* v, T* o, float* lse,
-                                          int64_t lse_at) {
-  // (everything by value: what this call is given by reference would live in local memory in the main loop)
+// A warp's rows whose stored results are not finite, again from the keys they see (rare: a NaN or an infinity
+// among the inputs): a walk over the CTA's items behind the last of them.  (Not within an item: a row takes 0.58 us a
+// key, a warp's 32 rows over 11000 keys outlast the 200 ms after which the other warps' waits for it give up.)
+template <typename T, int D, bool BIAS>
+__device__ __noinline__ void mod_fix_items(const ModFwdArgs& f, int t, int rt, const T* q, const T* k, const T* v, T* o,
+                                           float* lse) {
   const ModArgs& a = f.a;
-  const T* kh = k + batch * a.ks[0] + u * a.ks[1];
-  const T* vh = v + batch * a.vs[0] + u * a.vs[1];
-  const int32_t* kd = f.kdoc != nullptr ? f.kdoc + (int64_t)batch * f.nkb * 64 : nullptr;
-  while (bad != 0) {
-    const int lane = __ffs(bad) - 1;
-    bad &= bad - 1;
-    ModView view;
-    view.pos = __shfl_sync(0xffffffffu, pos, lane);
-    view.lim = __shfl_sync(0xffffffffu, lim, lane);
-    view.doc = __shfl_sync(0xffffffffu, doc, lane);
-    const float slope2 = __shfl_sync(0xffffffffu, slope, lane);
-    const int64_t qo = __shfl_sync(0xffffffffu, qoff, lane), oo = __shfl_sync(0xffffffffu, ooff, lane);
-    const int64_t la = __shfl_sync(0xffffffffu, lse_at, lane);
-    float m, l, acc[D / 32];
-    mod_exact_row<T, D>(a, q + qo, kh, vh, kd, view, slope2, (int64_t)first * 64,
-                        ((int64_t)first + nmax) * 64, m, l, acc);
-    if (f.po != nullptr) {
-      const int64_t at = (int64_t)(f.split0 + split) * f.all_rows + la;
-      mod_row_store<float, D>(f.po + at * D, acc);
-      if ((threadIdx.x & 31) == 0) f.pml[la * f.parts + f.split0 + split] = make_float2(m, l);
-    } else {
-      const float inv = l == 0.0f ? 0.0f : recip_refined(l);
+  __syncwarp();  // the rows' stores, by other lanes
+  for (int64_t kk = 0, w; (w = atm_item_of(kk, f.items)) >= 0; ++kk) {
+    const ModItem it(w, f);
+    if (it.nt(t) == 0) continue;
+    const ModRowAt x = mod_row_at<BIAS>(f, it, t, rt);
+    const int64_t ooff = it.b * a.os[0] + (int64_t)x.h * a.os[1] + x.i * a.os[2];
+    const int64_t part = f.split0 + it.split, pat = part * f.all_rows + x.lse_at;
+    bool lost = false;
+    if (x.in && f.po != nullptr) {
+      const float l = f.pml[x.lse_at * f.parts + part].y;
+      lost = l != l;
+      for (int c = 0; c < D && !lost; c += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(f.po + pat * D + c);
+        const float chk = __fmaf_rn(y.x, 0.0f, __fmaf_rn(y.y, 0.0f, __fmaf_rn(y.z, 0.0f, y.w * 0.0f)));
+        lost = chk != chk;
+      }
+    } else if (x.in) {
+      for (int c = 0; c < D && !lost; c += 8) {
+        float y[8], chk = 0.0f;
+        unpack16<T>(*reinterpret_cast<const uint4*>(o + ooff + c), y);
 #pragma unroll
-      for (int x = 0; x < D / 32; ++x) acc[x] *= inv;
-      mod_row_store<T, D>(o + oo, acc);
-      if (lse != nullptr && (threadIdx.x & 31) == 0) lse[la] = mod_lse(m, l);
+        for (int i = 0; i < 8; ++i) chk = __fmaf_rn(y[i], 0.0f, chk);
+        lost = chk != chk;
+      }
     }
-    __syncwarp();
+    uint32_t bad = __ballot_sync(0xffffffffu, lost);
+    while (bad != 0) {
+      const int lane = __ffs(bad) - 1;
+      bad &= bad - 1;
+      ModView view;
+      view.pos = __shfl_sync(0xffffffffu, x.rs.pos, lane);
+      view.lim = __shfl_sync(0xffffffffu, x.rs.lim, lane);
+      view.doc = __shfl_sync(0xffffffffu, x.rs.doc, lane);
+      const float slope2 = __shfl_sync(0xffffffffu, x.rs.slope2, lane);
+      const int64_t qo = __shfl_sync(0xffffffffu, x.qoff, lane), oo = __shfl_sync(0xffffffffu, ooff, lane);
+      const int64_t la = __shfl_sync(0xffffffffu, x.lse_at, lane), pa = __shfl_sync(0xffffffffu, pat, lane);
+      float m, l, acc[D / 32];
+      mod_exact_row<T, D>(a, q + qo, k + it.b * a.ks[0] + it.u * a.ks[1], v + it.b * a.vs[0] + it.u * a.vs[1],
+                          f.kdoc != nullptr ? f.kdoc + (int64_t)it.b * f.nkb * 64 : nullptr, view, slope2,
+                          (int64_t)it.first * 64, ((int64_t)it.first + it.nmax) * 64, m, l, acc);
+      if (f.po != nullptr) {
+        mod_row_store<float, D>(f.po + pa * D, acc);
+        if ((threadIdx.x & 31) == 0) f.pml[la * f.parts + part] = make_float2(m, l);
+      } else {
+        const float inv = l == 0.0f ? 0.0f : recip_refined(l);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) acc[i] *= inv;
+        mod_row_store<T, D>(o + oo, acc);
+        if (lse != nullptr && (threadIdx.x & 31) == 0) lse[la] = mod_lse(m, l);
+      }
+    }
   }
 }
 
@@ -751,39 +815,14 @@ __global__ void __launch_bounds__(AtmShape<2>::BLOCK, 1)
     // row threads: tile t, TMEM lane rt of the tile
     const int t = tid >> 7, rt = tid & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    bool redo = false;  // some row of the warp's items is not finite
     for (int64_t kk = 0, w; (w = atm_item_of(kk, f.items)) >= 0; ++kk) {
       const ModItem it(w, f);
       const int n = it.nt(t), nmax = t < tiles ? it.nmax : 0, r0 = R0, g0 = J;
-      const int64_t r = it.r0 + t * BM + rt;
-      const bool in = r < f.rows;
-      const int64_t rc = in ? r : f.rows - 1;  // rows past the end compute the last row's and store nothing
-      const int g = f.pf > 1 ? (int)((uint32_t)rc / (uint32_t)a.sq) : 0;
-      const int64_t i = rc - (int64_t)g * a.sq;
-      const int h = it.hp * f.pf + g;
-      ModRowState rs;
-      int64_t lse_at = ((int64_t)it.b * a.hq + h) * a.sq + i;
-      int64_t qoff = it.b * a.qs[0] + (int64_t)h * a.qs[1] + i * a.qs[2];
-      if (f.req > 0) {
-        const int per = f.map_group * f.map_sq, rq = (int)rc / per, rest = (int)rc - rq * per;
-        const int hg = rest / f.map_sq, tok = rest - hg * f.map_sq, hh = it.u * f.map_group + hg;
-        lse_at = ((int64_t)rq * f.map_hq + hh) * f.map_sq + tok;
-        if (f.q_req) qoff = (int64_t)rq * a.qs[0] + (int64_t)hh * a.qs[1] + tok * a.qs[2];
-        int64_t own = f.own_sk;
-        if (f.own_len != nullptr) {
-          const int64_t x = f.own_len[rq];
-          own = x < 0 ? 0 : (x < own ? x : own);
-        }
-        rs.pos = a.sk + own - f.map_sq + tok;
-        rs.lim = (int)a.sk;
-        rs.doc = 0;
-        rs.slope2 = BIAS ? a.slopes[hh] * L2E_HI : 0.0f;
-      } else {
-        const ModView view = mod_view(a, it.b, i);
-        rs.pos = view.pos;
-        rs.lim = (int)view.lim;
-        rs.doc = view.doc;
-        rs.slope2 = BIAS ? a.slopes[h] * L2E_HI : 0.0f;
-      }
+      const ModRowAt at_row = mod_row_at<BIAS>(f, it, t, rt);
+      const ModRowState& rs = at_row.rs;
+      const bool in = at_row.in;
+      const int64_t lse_at = at_row.lse_at;
       float m_ref = neg_inf(), l = 0.0f;
       const int4* kblock = f.kblock != nullptr ? f.kblock + (int64_t)it.b * f.nkb + it.first : nullptr;
       int4 docs = make_int4(0, 0, 0, 0);
@@ -824,7 +863,7 @@ __global__ void __launch_bounds__(AtmShape<2>::BLOCK, 1)
       // the item's output: whole rows normalised in the input type, or the
       // part's state in fp32.  chk stays 0 while every value is finite
       float chk = 0.0f;
-      const int64_t ooff = it.b * a.os[0] + (int64_t)h * a.os[1] + i * a.os[2];
+      const int64_t ooff = it.b * a.os[0] + (int64_t)at_row.h * a.os[1] + at_row.i * a.os[2];
       if (f.po != nullptr) {
         const int64_t at = (int64_t)(f.split0 + it.split) * f.all_rows + lse_at;
         if (n > 0) {
@@ -906,10 +945,7 @@ __global__ void __launch_bounds__(AtmShape<2>::BLOCK, 1)
         }
         if (in && lse != nullptr) lse[lse_at] = mod_lse(m_ref, l);
       }
-      const uint32_t bad = __ballot_sync(0xffffffffu, in && n > 0 && (chk != 0.0f || chk != chk || l != l));
-      if (bad != 0)
-        mod_fix_rows<T, D>(bad, f, it.b, it.u, it.first, it.nmax, it.split, rs.pos, rs.lim, rs.doc, rs.slope2,
-                           qoff, ooff, q, k, v, o, lse, lse_at);
+      redo |= __any_sync(0xffffffffu, in && n > 0 && (chk != 0.0f || chk != chk || l != l));
       // the blocks that only the other tile has: in step with the issuing warp
       for (int b = n; b < nmax; ++b) {
         const int gg = g0 + b, rr = r0 + b;
@@ -922,6 +958,7 @@ __global__ void __launch_bounds__(AtmShape<2>::BLOCK, 1)
       }
       advance(it);
     }
+    if (redo) mod_fix_items<T, D, BIAS>(f, t, rt, q, k, v, o, lse);
   }
   if (!ok) atomicOr(f.status, DEV_TIMEOUT);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
