@@ -88,18 +88,22 @@ struct MbwCols {
   uint32_t stats;         // MODE_DKV: shared address of the 32 columns' lse2
 };
 
-// P of the thread's 32 columns from the raw products y: p, and packed in the input type pk2. With a cap
-// MODE_DKV needs P (1 - t^2) alone further on (p holds that), MODE_DQ both: w2 keeps 1 - t^2 as fp16 pairs.
-// (The factor itself, not t^2: it is off by 2^-11 of its value at most, what dS's own rounding costs in fp16 and
-// an eighth of that in bf16, and by 2^-25 where it is subnormal, less than t's own last bit leaves of it.  t^2 in fp16
-// would be off by 2^-12 beside a factor that vanishes at the cap: dq was up to 149 times its bound.)
+// P of the thread's 32 columns from the raw products y: p, and packed in the input type pk2.  With a cap p holds
+// P (1 - t^2), all that dS needs; MODE_DQ's r = sum P (dP - D) takes the rest of P beside it: t2 keeps P t^2 2^14 as fp16
+// pairs (in 32 bits they would take 16 registers more, which spill).  Off by 2^-11 of P t^2 and, scaled, never
+// subnormal where it matters, they blur the correction of D alone, by 2^-11 sum P t^2 |dP - D|.  (dS itself takes no
+// rounding but its own: with 1 - t^2 in fp16 it was off by sqrt 2 as much in fp16, with t^2 in fp16 by up to 149 times
+// its bound where scores reach the cap.)
+constexpr float MBW_T = 128.0f;  // MODE_DQ holds t times this, t^2 times its square
 template <typename T, int MODE, bool CAP, bool BIAS, int FORM, bool BORDER, int LINE>
 __device__ __forceinline__ void mbw_probs(float (&p)[32], const ModArgs& a, const MbwCols& q,
-                                          uint32_t (&w2)[CAP && MODE == MODE_DQ ? 16 : 1], uint32_t (&pk2)[16]) {
+                                          uint32_t (&t2)[CAP && MODE == MODE_DQ ? 16 : 1], uint32_t (&pk2)[16]) {
   // LINE: 1 the distance falls (MODE_DQ) or rises along the columns, 0 it turns within them
   const float step = MODE == MODE_DQ ? -1.0f : 1.0f;
   const float st = -q.slope2 * step, base = -q.slope2 * q.d0;
-  const unsigned long long c2 = pk(a.c, a.c), k2 = pk(a.cap2, a.cap2), st2 = pk(2.0f * st, 2.0f * st);
+  constexpr float TS = CAP && MODE == MODE_DQ ? MBW_T : 1.0f;
+  const float k = a.cap2 * (1.0f / TS);
+  const unsigned long long c2 = pk(a.c, a.c), k2 = pk(k, k), st2 = pk(2.0f * st, 2.0f * st);
   const unsigned long long nl = pk(-q.lse2, -q.lse2);
   unsigned long long line = 0;  // stepped, anew every 8 columns
 #pragma unroll
@@ -116,9 +120,9 @@ __device__ __forceinline__ void mbw_probs(float (&p)[32], const ModArgs& a, cons
       unsigned long long t;
       const unsigned long long u = mul2(pk(v0 ? p[x] : 0.0f, v1 ? p[x + 1] : 0.0f), c2);
       if constexpr (FORM == CAP_EXP)
-        t = pk(tanh_exp(pk_lo(u)), tanh_exp(pk_hi(u)));
+        t = pk(tanh_exp(pk_lo(u), TS), tanh_exp(pk_hi(u), TS));
       else
-        t = mul2(tanh_ratio2<FORM == CAP_NEAR>(u, 1.0f), u);
+        t = mul2(tanh_ratio2<FORM == CAP_NEAR>(u, TS), u);
       tt = mul2(t, t);
       e = fma2(t, k2, sub);
     } else {
@@ -143,16 +147,17 @@ __device__ __forceinline__ void mbw_probs(float (&p)[32], const ModArgs& a, cons
     if constexpr (!CAP) {
       pk2[x / 2] = pack2<T>(p0, p1);
     } else {
-      const unsigned long long w = fma2(tt, pk(-1.0f, -1.0f), pk(1.0f, 1.0f));
-      const unsigned long long pd = mul2(pk(p0, p1), w);
+      constexpr float one = 1.0f / (TS * TS);
+      const unsigned long long pp = pk(p0, p1), pd = mul2(pp, fma2(tt, pk(-one, -one), pk(1.0f, 1.0f)));
+      p[x] = pk_lo(pd);
+      p[x + 1] = pk_hi(pd);
       if constexpr (MODE == MODE_DKV) {
         pk2[x / 2] = pack2<T>(p0, p1);
-        p[x] = pk_lo(pd);
-        p[x + 1] = pk_hi(pd);
       } else {
         // X1 takes P (1 - t^2): the correction it serves is one of dS
-        pk2[x / 2] = pack2<T>(pk_lo(pd), pk_hi(pd));
-        w2[x / 2] = pack2<__half>(pk_lo(w), pk_hi(w));
+        pk2[x / 2] = pack2<T>(p[x], p[x + 1]);
+        const unsigned long long rest = mul2(pp, tt);
+        t2[x / 2] = pack2<__half>(pk_lo(rest), pk_hi(rest));
       }
     }
   }
@@ -160,22 +165,22 @@ __device__ __forceinline__ void mbw_probs(float (&p)[32], const ModArgs& a, cons
 
 template <typename T, int MODE, bool CAP, bool BIAS, int FORM, bool BORDER>
 __device__ __forceinline__ void mbw_probs_line(float (&p)[32], const ModArgs& a, const MbwCols& q, int line,
-                                               uint32_t (&w2)[CAP && MODE == MODE_DQ ? 16 : 1], uint32_t (&pk2)[16]) {
+                                               uint32_t (&t2)[CAP && MODE == MODE_DQ ? 16 : 1], uint32_t (&pk2)[16]) {
   if constexpr (!BIAS) {
-    mbw_probs<T, MODE, CAP, BIAS, FORM, BORDER, 0>(p, a, q, w2, pk2);
+    mbw_probs<T, MODE, CAP, BIAS, FORM, BORDER, 0>(p, a, q, t2, pk2);
   } else {
     // (a line that rises against the usual direction takes the general form)
     if (__builtin_expect(line > 0, 1))
-      mbw_probs<T, MODE, CAP, BIAS, FORM, BORDER, 1>(p, a, q, w2, pk2);
+      mbw_probs<T, MODE, CAP, BIAS, FORM, BORDER, 1>(p, a, q, t2, pk2);
     else
-      mbw_probs<T, MODE, CAP, BIAS, FORM, BORDER, 0>(p, a, q, w2, pk2);
+      mbw_probs<T, MODE, CAP, BIAS, FORM, BORDER, 0>(p, a, q, t2, pk2);
   }
 }
 
 // Scores to P, over the first 16 of the score columns they came from
 template <typename T, int MODE, bool CAP, bool BIAS>
 __device__ __forceinline__ void mbw_phase1(uint32_t ts, const ModArgs& a, const MbwCols& q, bool border, int line,
-                                           float (&p)[32], uint32_t (&w2)[CAP && MODE == MODE_DQ ? 16 : 1]) {
+                                           float (&p)[32], uint32_t (&t2)[CAP && MODE == MODE_DQ ? 16 : 1]) {
   tc_ld32(ts, p);
   int form = CAP_EXP;
   if constexpr (CAP) {
@@ -188,16 +193,16 @@ __device__ __forceinline__ void mbw_phase1(uint32_t ts, const ModArgs& a, const 
   }
   uint32_t pk2[16];
   if (__builtin_expect(!border && (!CAP || form == CAP_NEAR), 1)) {
-    mbw_probs_line<T, MODE, CAP, BIAS, CAP_NEAR, false>(p, a, q, line, w2, pk2);
+    mbw_probs_line<T, MODE, CAP, BIAS, CAP_NEAR, false>(p, a, q, line, t2, pk2);
   } else if (border) {
     if (CAP && form != CAP_EXP)
-      mbw_probs_line<T, MODE, CAP, BIAS, CAP_POLY, true>(p, a, q, line, w2, pk2);
+      mbw_probs_line<T, MODE, CAP, BIAS, CAP_POLY, true>(p, a, q, line, t2, pk2);
     else
-      mbw_probs_line<T, MODE, CAP, BIAS, CAP_EXP, true>(p, a, q, line, w2, pk2);
+      mbw_probs_line<T, MODE, CAP, BIAS, CAP_EXP, true>(p, a, q, line, t2, pk2);
   } else if (CAP && form == CAP_POLY) {
-    mbw_probs_line<T, MODE, CAP, BIAS, CAP_POLY, false>(p, a, q, line, w2, pk2);
+    mbw_probs_line<T, MODE, CAP, BIAS, CAP_POLY, false>(p, a, q, line, t2, pk2);
   } else if (CAP) {
-    mbw_probs_line<T, MODE, CAP, BIAS, CAP_EXP, false>(p, a, q, line, w2, pk2);
+    mbw_probs_line<T, MODE, CAP, BIAS, CAP_EXP, false>(p, a, q, line, t2, pk2);
   }
   tc_st16u(ts, pk2);
 }
@@ -205,7 +210,7 @@ __device__ __forceinline__ void mbw_phase1(uint32_t ts, const ModArgs& a, const 
 // dS = P (1 - t^2) (dP - D) over the first 16 columns of the dP it came from; MODE_DQ: r += P (dP - D)
 template <typename T, int MODE, bool CAP>
 __device__ __forceinline__ void mbw_phase2(uint32_t tdp, float delta, uint32_t stats, const float (&p)[32],
-                                           const uint32_t (&w2)[CAP && MODE == MODE_DQ ? 16 : 1], float& r) {
+                                           const uint32_t (&t2)[CAP && MODE == MODE_DQ ? 16 : 1], float& r) {
   const unsigned long long nd = pk(-delta, -delta);
   unsigned long long acc[2] = {0ull, 0ull};
   float dp[32];
@@ -219,18 +224,19 @@ __device__ __forceinline__ void mbw_phase2(uint32_t tdp, float delta, uint32_t s
       asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(l0), "=f"(l1) : "r"(stats + 4 * x));
       sub = pk(-l0, -l1);
     }
-    const unsigned long long v = add2(pk(dp[x], dp[x + 1]), sub), pp = pk(p[x], p[x + 1]);
-    if constexpr (MODE == MODE_DQ) acc[(x >> 1) & 1] = fma2(pp, v, acc[(x >> 1) & 1]);
-    unsigned long long d = mul2(pp, v);
+    const unsigned long long v = add2(pk(dp[x], dp[x + 1]), sub), d = mul2(pk(p[x], p[x + 1]), v);
     if constexpr (CAP && MODE == MODE_DQ) {
-      const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&w2[x / 2]));
-      d = mul2(d, pk(w.x, w.y));
+      const float2 rest = __half22float2(*reinterpret_cast<const __half2*>(&t2[x / 2]));
+      acc[0] = add2(acc[0], d);
+      acc[1] = fma2(pk(rest.x, rest.y), v, acc[1]);
+    } else if constexpr (MODE == MODE_DQ) {
+      acc[(x >> 1) & 1] = fma2(pk(p[x], p[x + 1]), v, acc[(x >> 1) & 1]);
     }
     ds[x / 2] = pack2<T>(pk_lo(d), pk_hi(d));
   }
   tc_st16u(tdp, ds);
   if constexpr (MODE == MODE_DQ)
-    r += (pk_lo(acc[0]) + pk_hi(acc[0])) + (pk_lo(acc[1]) + pk_hi(acc[1]));
+    r += __fmaf_rn(CAP ? 1.0f / (MBW_T * MBW_T) : 1.0f, pk_lo(acc[1]) + pk_hi(acc[1]), pk_lo(acc[0]) + pk_hi(acc[0]));
 }
 
 // 64 bytes (pkd) of each of a warp's 32 rows through its 2 KB of shared memory, so that the stores go out
@@ -600,17 +606,17 @@ __global__ void __launch_bounds__(MBW_THREADS, 1)
         line = __all_sync(0xffffffffu, ahead) ? 1 : 0;
       }
       float p[32];
-      uint32_t w2[CAP && MODE == MODE_DQ ? 16 : 1];
+      uint32_t t2[CAP && MODE == MODE_DQ ? 16 : 1];
       wait_or_flag(B_S + grp, (uint32_t)((i >> 1) & 1));
       if constexpr (MODE == MODE_DKV) wait_or_flag(B_C1 + i % NST, (uint32_t)((i / NST) & 1));  // the statistics
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      mbw_phase1<T, MODE, CAP, BIAS>(ts, a, cq, border, line, p, w2);
+      mbw_phase1<T, MODE, CAP, BIAS>(ts, a, cq, border, line, p, t2);
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_P + grp));
       wait_or_flag(B_DP + grp, (uint32_t)((i >> 1) & 1));
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      mbw_phase2<T, MODE, CAP>(tdp, delta, stats + 256, p, w2, r);
+      mbw_phase2<T, MODE, CAP>(tdp, delta, stats + 256, p, t2, r);
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_DS + grp));

@@ -124,11 +124,11 @@ struct TanhPoly<false> {
     return v[i];
   }
 };
-// tanh over the whole range, 1 - 2 / (1 + e^(2u)): absolute error within 2^-22
-__device__ __forceinline__ float tanh_exp(float u) {
+// scale tanh over the whole range, 1 - 2 / (1 + e^(2u)): absolute error within 2^-22 scale
+__device__ __forceinline__ float tanh_exp(float u, float scale = 1.0f) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2_full(u * 2.8853900817779268f)));
-  return __fmaf_rn(-2.0f, r, 1.0f);
+  return __fmaf_rn(-2.0f * scale, r, scale);
 }
 // scale tanh(u) / u of a pair (the scale rides on the coefficients)
 template <bool NEAR>

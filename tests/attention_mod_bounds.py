@@ -18,11 +18,12 @@ w = 1 - t^2; 1 and 0 in their place without a cap):
   D          o as it was rounded is off by e_o = |do| . (bound of o) + u (D + 2) |do|.|o|; corrected by
              r = sum_j P (dP - D), which leaves
              e_d = p_i sum_j P |dP - D| + sum_j P (u (D + 2) |do|.|v| + u (n + 16) (|dP| + |D|))
+                   + 2^-11 sum_j P t^2 |dP - D| + 2^-39 sum_j (|dP| + |D|)
+             (with a cap r takes P t^2 2^14 as fp16, which steps by 2^-10, half of it is the rounding, and by 2^-24 where
+             it is subnormal)
   dS         (h + p_i) |dS| + z + 2^-126 w (|dP| + |D|) + P w (u (D + 2) |do|.|v| + e_d + 2 h e_o + 16 u (|dP| + |D|))
              + P e_w (|dP| + |D|)
              (2 h e_o: dS is rounded to the type before the correction, and so is the P w that carries it)
-  dS for dq  the factor w is kept as fp16 between two steps: 2^-11 |dS| more (fp16 steps by 2^-10, half of it is the
-             rounding), and 2^-25 P (|dP| + |D|) where it is subnormal (steps of 2^-24)
   dq         scale (sum_j e_dS |k| + u n sum_j |dS| |k|) + h |dq| + z;  dk likewise over i
 """
 import math
@@ -89,11 +90,12 @@ def reference(q, k, v, scale, seen, pos, softcap=0.0, slopes=None, d_o=None):
     prod = U * (D + 2) * (gd.abs() @ vd.abs().transpose(-1, -2))
     eo = (gd.abs() * ob).sum(-1, keepdim=True) + U * (D + 2) * (gd.abs() * o.abs()).sum(-1, keepdim=True)
     ed = pi * (p * (dP - delta).abs()).sum(-1, keepdim=True) + (p * (prod + U * (m + 16) * size)).sum(-1, keepdim=True)
+    if softcap > 0:
+        ed = ed + (2.0 ** -11 * p * (1 - w) * (dP - delta).abs() + 2.0 ** -39 * size).sum(-1, keepdim=True)
     dsb = (h + pi) * dS.abs() + torch.where(sn, z, 0.0) + 2.0 ** -126 * w * size \
         + p * w * (prod + ed + 2 * h * eo + 16 * U * size) + p * ew * size
-    dqs = dsb + (2.0 ** -11 * dS.abs() + 2.0 ** -25 * p * size if softcap > 0 else 0.0)
     dq = scale * (dS @ kd)
-    dqb = scale * ((dqs + U * m * dS.abs()) @ kd.abs()) + h * dq.abs() + z
+    dqb = scale * ((dsb + U * m * dS.abs()) @ kd.abs()) + h * dq.abs() + z
     dk = scale * group(dS.transpose(-1, -2) @ qd)
     dkb = scale * group((dsb + U * n * dS.abs()).transpose(-1, -2) @ qd.abs()) + h * dk.abs() + z
     out.update(dq=(dq, dqb), dk=(dk, dkb), dv=(dv, dvb + h * dv.abs() + z))

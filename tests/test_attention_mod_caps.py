@@ -82,3 +82,19 @@ def test_gradients_where_a_cap_saturates(std, cap, n, m, D, dt):
     q, k, v, d_o, _ = make(int(std) + n, 2, 4, 2, n, m, D, dt, std=std)
     compare(q, k, v, d_o, causal=m >= n, softcap=cap)
     compare(q, k, v, d_o, causal=m >= n, softcap=cap, slopes=slopes_of(4))
+
+
+@pytest.mark.parametrize("std,cap", [(3.0, 20.0), (3.0, 0.0), (20.0, 20.0)])
+def test_dq_takes_two_roundings(std, cap):
+    """In fp16 dS is rounded once and dq once, whether scores are capped or not.  A rounding to fp16 is off by a uniform
+    part of half a step, 2^-11 / m of a value of mantissa m: over mantissas in [1, 2) with density 1 / (m ln 2) its root
+    mean square is 2^-11 / sqrt(3) sqrt(3 / (8 ln 2)) = 2.07e-4, and errors of many independent terms add up as the
+    terms do.  Two of them make 2.93e-4 of dq's norm, three 3.59e-4; the limit lies between."""
+    q, k, v, d_o, _ = make(int(std + cap), 2, 4, 2, 512, 512, 64, "f16", std=std)
+    o, lse = smx.attention_mod_forward(q, k, v, softcap=cap)
+    dq = smx.attention_mod_backward(q, k, v, o, lse, d_o, softcap=cap)[0].double()
+    seen, pos = ref.visible(2, 512, 512, q.device)
+    want = bounds.reference(q, k, v, 0.125, seen, pos, cap, None, d_o)["dq"][0]
+    off = float((dq - want).norm() / want.norm())
+    print(off)
+    assert off <= 3.25e-4
