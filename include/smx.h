@@ -301,8 +301,12 @@ smx_status smx_attention_forward(const void *q, const void *k, const void *v, vo
  *   scores are all -inf, is the declared empty row: o = 0, lse = -inf.  A NaN or +inf
  *   among a row's visible scores makes the row NaN (lse NaN).  Keys that a query does not
  *   see add nothing to its row, whatever their stored values are
- *   (NaN and infinities included): padding may hold anything (beside such values a row may
- *   be computed with other, not worse, intermediate roundings, and more slowly).
+ *   (NaN and infinities included): padding may hold anything.  What lies behind k_len costs
+ *   nothing.  A NaN or an infinity in another place that is not seen (ahead of a causal row, in
+ *   another document) has the rows beside it computed again one key after the other: with other, not
+ *   worse, intermediate roundings, and far more slowly (some 0.6 us a key and row).  So has, in the
+ *   backward, a finite score gradient beyond the type's range (fp16: P |dP - D| above 65504, where an
+ *   upstream gradient was scaled up).
  * Scores, statistics and sums are fp32; probabilities (and, backward, the
  * score gradients) enter the second products rounded to the input type.
  * Results do not depend on timing: every sum has a fixed order.
@@ -345,6 +349,11 @@ smx_status smx_attention_mod_workspace(const smx_attention_mod *p, int backward,
  *              (NULL when that is 0), overlapping nothing else.
  * A handful of query rows over many keys (single tokens) and long prompts both take
  * kernels made for them, with the keys split over the device where there are few rows.
+ * Up to 32 query rows a key head (query heads of its group x seq_q) read every key up to
+ * their limit: blocks without a key of their documents are skipped above that only.  Above it, the
+ * query heads of a group share the reading of their keys where their rows lie behind each other
+ * (q_stride[head] == seq_q * q_stride[row]); 257 rows of 16 heads over 2 key heads of 65536 keys
+ * take 184 us so, and 320 as [batch][rows][heads][head_dim].
  */
 smx_status smx_attention_mod_forward(const smx_attention_mod *p, const void *q, const void *k, const void *v,
                                      void *o, float *lse, void *workspace, int64_t workspace_bytes,
@@ -357,7 +366,8 @@ smx_status smx_attention_mod_forward(const smx_attention_mod *p, const void *q, 
  *     dS_ij = P_ij (do_i . v_j - D_i) (1 - (x_ij / softcap)^2 where capped)
  *     dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum_i dS_ij q_i,   dv_j = sum_i P_ij do_i
  * where a key head's sums run over every query head of its group.  slopes are constants.
- *   o, lse     the forward's results for these arguments.
+ *   o, lse     the forward's results for these arguments: of exactly these keys (sum_j P_ij = 1 is
+ *              used), not of rows joined from several calls.
  *   d_o        the upstream gradient, dtype; dq, dk, dv: written, dtype.
  * Rows that see no key have dq = 0; keys that no query sees have dk = dv = 0. A
  * NaN in a row spreads to that row's dq and to the dk, dv of the keys it sees.

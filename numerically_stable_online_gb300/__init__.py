@@ -588,7 +588,7 @@ def attention_mod_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o:
                            dk: torch.Tensor | None = None, dv: torch.Tensor | None = None, stream=None):
     """(dq, dk, dv) of sum(d_o * o) through attention_mod_forward, from its o and lse and the same arguments.
 
-    The gradients of shared key heads are their groups' sums; results do not depend on timing.
+    o and lse must be that call's own: rows joined from several calls over parts of the keys are not taken.  The gradients of shared key heads are their groups' sums; results do not depend on timing.
     """
     return _on_device(_mod_backward, q.get_device(), stream, q, k, v, o, lse, d_o, dq, dk, dv, scale, causal,
                       softcap, slopes, prefix_len, q_doc, k_doc, k_len, q_start)

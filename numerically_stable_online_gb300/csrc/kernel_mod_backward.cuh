@@ -29,10 +29,11 @@
 //
 // A lane whose result is not finite is computed again from the pairs that are visible
 // (kernel_mod_exact.cuh).  Bound: at D = 128 the products, four a block (1280 tensor cycles, the 64-column ones at two
-// thirds of the full rate; S and dP are formed in both kernels, and MODE_DQ's X1 is the correction's); at D = 64 the
-// row threads.  16 heads x 8192 rows, causal: 689 us at
-// D = 128 (997 TFLOP/s of the five products of the formulas), 625 us at D = 64; every key 1340 us;
-// capped causal 864, slopes 717; documents of 900 rows 201.
+// thirds of the full rate; S and dP are formed in both kernels, and MODE_DQ's X1 is the correction's) beside the row
+// threads (capped: tensor pipe busy 49 to 54 % of the time, issue slots 57, exp2 unit 14); at D = 64 the row threads
+// (documents and bias: tensor pipe 24 %, issue slots 44).  16 heads x 8192 rows, causal, calls back to back: 699 us at
+// D = 128 (983 TFLOP/s of the five products of the formulas), 619 us at D = 64; every key 1430 us;
+// capped causal 885 (1000 where scores reach the cap), slopes 729; documents of 900 rows 201.
 #pragma once
 
 #include "kernel_mod_exact.cuh"

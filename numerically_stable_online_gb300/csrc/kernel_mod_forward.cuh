@@ -19,11 +19,15 @@
 //   - a row whose result is not finite is computed again from the keys it sees, behind the CTA's items
 //     (mod_fix_items, kernel_mod_exact.cuh): a product's 0 x NaN from a key that the row does not see leaves no trace.
 //
-// Bound: at D = 128 the tensor cores (2 x 32 heads x 4096 rows: 369 us, 1490 TFLOP/s; causal 211 us); a cap, a bias or
-// D = 64 makes it the row warps' arithmetic (the exp2 unit and issue slots; capped 629 us, causal 357; slopes 524,
-// causal 335; D = 64: 338).  The issuing and rare code is kept short: what the instruction cache loses between
-// blocks or items is fetched anew (capped rows in two rolled passes with a maximum before the cap: 379 us where one
-// unrolled pass took 415; an item's output in rolled loops and its decoding by 32-bit divisions: causal 211, before 234).
+// Bound: at D = 128 the tensor cores (2 x 32 heads over 8 key heads x 4096 rows, calls back to back: 373 us, 1470
+// TFLOP/s; causal 217); with a cap (631, causal 360), a bias (530, causal 340) or D = 64 (341) the row warps' chain: a
+// block's load from tensor memory, maximum, exponentials, store and hand-over, two warps a scheduler.  No unit is full
+// then: a causal capped forward has its tensor pipe busy 31 % of the time, its issue slots 47, exp2 unit 16, FMA pipe 20
+// (ncu; the exp2 unit gives 32 a cycle an SM, so 128 x 64 scores take it 256 cycles).  The issuing and rare code is
+// kept short: what the instruction cache loses between blocks or items is fetched anew (its hit rate is 89 to 97 %, and
+// about one of a scheduler's warps waits for instructions; capped rows in two rolled passes with a maximum before the
+// cap: 379 us where one unrolled pass took 415; an item's output in rolled loops and its decoding by 32-bit divisions:
+// causal 211, before 234).
 #pragma once
 
 #include "kernel_attention_tma.cuh"
