@@ -308,7 +308,8 @@ smx_status smx_attention_forward(const void *q, const void *k, const void *v, vo
  *   backward, a finite score gradient beyond the type's range (fp16: P |dP - D| above 65504, where an
  *   upstream gradient was scaled up).
  * Scores, statistics and sums are fp32; probabilities (and, backward, the
- * score gradients) enter the second products rounded to the input type.
+ * score gradients) enter the second products rounded to the input type.  (Values at the very end of
+ * their type may round over it: fp16 beyond 65472, bf16 where up to 2^8 sum_j |v_j| passes 2^128.)
  * Results do not depend on timing: every sum has a fixed order.
  *
  * Sizes: heads_q a multiple of heads_kv; head_dim 64 or 128 (else
